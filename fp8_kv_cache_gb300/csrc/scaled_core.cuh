@@ -10,13 +10,15 @@
 // to the second product stay in [0, 1] whatever the scales' range, and
 //     out = sum p_t vc_t / sum p_t / vs_t.
 // (n is a reference that the maximum may pass by 2^kSlack before the sums are
-// rescaled: weights of up to 2^kSlack instead of 1.)  The weights are rounded to
-// binary16 (11 bits; the sums stay in float32).  They are fed as 2^kShift p_t:
-// binary16 is normal down to 2^-14, which then stands for 2^-(14 + kShift), so
-// the many small weights of a long context keep their 11 bits.  The denominator
-// is summed from the unrounded weights.  Scales below 2^-80 count as 2^-80 in
-// log2 vs: their values are zeros in binary16 either way, and the denominator
-// stays finite.
+// rescaled: weights of up to 2^kSlack instead of 1.)  The second product takes
+// binary16, so a weight is fed as the sum of two such numbers, its rounding and the
+// rounding of what that leaves: 22 bits, below the float32 errors of the scores.
+// (One number, 11 bits, moved outputs by as much as their own rounding to binary16
+// does: 64 tokens, errors of 2.5e-4 instead of 2.1e-4; prefill took 378 us for the
+// 414 below, decode 6.6 for 6.9.)  They are fed as 2^kShift p_t: binary16's steps
+// end at 2^-24, which then stands for 2^-(24 + kShift).  The denominator is summed
+// from the float32 weights.  Scales below 2^-80 count as 2^-80 in log2 vs: their
+// values are zeros in binary16 either way, and the denominator stays finite.
 //
 // Data path of a warp: a private ring of two 16-token tiles filled by 16-byte
 // cp.async (rows of tokens that are not attended are filled with zeros), the 16
@@ -26,12 +28,13 @@
 // their rows.
 //
 // Bound where the codes come from L2 (prefill): instructions.  4096 rows x 2050
-// E4M3 tokens x 6 heads take 378 us; 408 us with 64-bit row offsets and four chains
-// of score sums; 531 us also with fills of half tiles, a joint maximum over the lanes
-// for every tile (now only when one passes the reference by 2^kSlack) and V's bytes
-// paired by permutes; 80 us more with a select for every fragment of a row and a
-// rescale whenever a maximum grew.  A variant of the fill for tiles whose tokens are
-// all attended gains nothing (385 us: more code).
+// E4M3 tokens x 6 heads take 414 us.  At one binary16 number a weight they took 378
+// us; 408 us with 64-bit row offsets and four chains of score sums; 531 us also with
+// fills of half tiles, a joint maximum over the lanes for every tile (now only when
+// one passes the reference by 2^kSlack) and V's bytes paired by permutes; 80 us more
+// with a select for every fragment of a row and a rescale whenever a maximum grew.  A
+// variant of the fill for tiles whose tokens are all attended gained nothing (385 us:
+// more code).
 #pragma once
 
 #include <cfloat>
@@ -263,9 +266,15 @@ struct Core {
         d0 += p[0] * iv0 + p[2] * iv1;
         d1 += p[1] * iv0 + p[3] * iv1;
         // ---- P fragments: transpose the two 8x8 blocks [token][head] -> [head][token]
-        uint32_t pb0, pb1;
-        asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(pb0) : "r"(pack_half2(p[0], p[1])));
-        asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(pb1) : "r"(pack_half2(p[2], p[3])));
+        uint32_t pb[2], rest[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t h = pack_half2(p[2 * i], p[2 * i + 1]);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+            const uint32_t l = pack_half2(p[2 * i] - f.x, p[2 * i + 1] - f.y);
+            asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(pb[i]) : "r"(h));
+            asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(rest[i]) : "r"(l));
+        }
         // ---- O^T += V^T P^T, 32 dims at a time
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -276,7 +285,8 @@ struct Core {
                 uint32_t a0, a1, a2, a3;
                 codes_to_f16<kInt8>(r[2 * j], a0, a2);
                 codes_to_f16<kInt8>(r[2 * j + 1], a1, a3);
-                mma16816(acc[2 * i + j], a0, a1, a2, a3, pb0, pb1);
+                mma16816(acc[2 * i + j], a0, a1, a2, a3, pb[0], pb[1]);
+                mma16816(acc[2 * i + j], a0, a1, a2, a3, rest[0], rest[1]);
             }
         }
     }

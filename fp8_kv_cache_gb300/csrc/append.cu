@@ -6,7 +6,8 @@
 // quotient by a power of two is exact; for INT8 the nearest integer of x inv,
 // inv ~ 1 / s, is corrected by the exact remainder x - q s (encode8).  A block
 // that holds rows already keeps the larger of the two scales and codes those rows
-// again when it grew.
+// again when it grew.  A stored scale may be smaller than any made here: units for
+// which that arithmetic is not exact take a longer way.
 //
 // Bound: HBM, each source row read once and its codes written once (8190 rows x 4
 // heads x K and V: 6.4 us; it takes 15.4 us for E4M3 in blocks of 64, 18.3 us for
@@ -158,7 +159,7 @@ __device__ __forceinline__ float block_scale(float m)
     return __uint_as_float((uint32_t)max(e, 1) << 23);
 }
 
-// The multiplier the quantiser takes for scale s (E4M3: exact).
+// The multiplier encode8 takes for scale s.
 __device__ __forceinline__ float inverse_scale(float s)
 {
     return s > 0.f ? __fdiv_rn(1.f, s) : 0.f;
@@ -185,6 +186,22 @@ __device__ __forceinline__ uint32_t int8_code(float x, float s, float inv)
     return (uint32_t)(int)fminf(fmaxf(q, -127.f), 127.f) & 0xFFu;
 }
 
+// x / s (s > 0, |x| <= 448 s or infinite or NaN) rounded to odd, so that the rounding
+// to E4M3 is the exact quotient's.  s = m 2^e and x 2^-e, of which no bit that could
+// matter is lost, take the division's remainder away from the subnormals.
+__device__ __forceinline__ float quotient_odd(float x, float s)
+{
+    if (!(fabsf(x) <= FLT_MAX))
+        return x;
+    int e;
+    const float m = frexpf(s, &e), y = scalbnf(x, -e);
+    const float q = __fdiv_rn(y, m), r = fmaf(-q, m, y);
+    uint32_t b = __float_as_uint(q);
+    if (r != 0.f && (b & 1u) == 0u)
+        b += ((r > 0.f) == (q > 0.f)) ? 1u : 0xFFFFFFFFu;
+    return __uint_as_float(b);
+}
+
 // A lane's 8 codes of x / s for any elements and s; out of line, for rows that
 // are not plain.
 template <class T>
@@ -197,7 +214,34 @@ __device__ __noinline__ uint2 int8_codes(Row<T> x, float s, float inv)
     return make_uint2(c[0], c[1]);
 }
 
-// A lane's 8 codes of finite elements and an ordinary s.  INT8: adding 1.5 2^23
+template <class T>
+__device__ __forceinline__ uint2 int8_row(const T* row, float s, float inv)
+{
+    Row<T> x;
+    x.load(row, threadIdx.x & 31);
+    return int8_codes(x, s, inv);
+}
+
+// The same of E4M3, for rows whose scale is not plain: one element (at x) after
+// another to its code (at to), without a call, which would make the kernels spill.
+template <class T>
+__device__ __forceinline__ void e4m3_codes(unsigned char* to, const T* x, float s)
+{
+#pragma unroll 1
+    for (int e = 0; e < 8; ++e)
+        to[e] = (unsigned char)e4m3x2(quotient_odd((float)x[e], s), 0.f);
+}
+
+// Whether encode8 codes a unit right whose new elements are finite or not and whose
+// scale is s: INT8 where s, s / 2 and 1 / s are far from the subnormals, E4M3 where
+// 1 / s is finite.
+template <bool kInt8>
+__device__ __forceinline__ bool is_plain(bool finite, float s)
+{
+    return kInt8 ? finite && s >= 1e-30f : s >= FLT_MIN || s == 0.f;
+}
+
+// A lane's 8 codes of a plain unit's elements.  INT8: adding 1.5 2^23
 // to x inv rounds to the nearest integer, in the low byte, and is within one of
 // the quotient's; the exact remainders say whether one of the eight is off
 // (their largest is half a step or more: rare, and a matter of ties).
@@ -278,14 +322,6 @@ __device__ __noinline__ uint2 int8_recode_small(uint2 w, float old, float s)
         r[e >> 2] |= ((uint32_t)(int)rint((double)c * (double)old / (double)s) & 0xFFu) << (8 * (e & 3));
     }
     return make_uint2(r[0], r[1]);
-}
-
-template <class T>
-__device__ __forceinline__ uint2 int8_row(const T* row, float s, float inv)
-{
-    Row<T> x;
-    x.load(row, threadIdx.x & 31);
-    return int8_codes(x, s, inv);
 }
 
 // Eight stored codes of scale `old`, coded again for scale s (inv = 1 / s).
@@ -453,8 +489,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps<T>, append_ctas<T>(H)) appen
             float* scale = a.scales[side] + page * a.sc.page + sb * a.sc.block_stride + j * a.sc.head;
             float old = held > 0 && active ? *scale : 0.f;
             uint32_t mm = unit_max<kWarpsPer>(Row<T>::top_of(m), red);
-            bool plain = Row<T>::finite(mm);
-            if (__syncthreads_or(!plain)) {
+            const bool finite = Row<T>::finite(mm);
+            if (__syncthreads_or(!finite)) {
                 // again, finite elements only
                 m = 0u;
                 for (int i = 0; i < mine; ++i) {
@@ -479,7 +515,6 @@ __global__ void __launch_bounds__(32 * kAppendWarps<T>, append_ctas<T>(H)) appen
             }
             const float s = fmaxf(fmaxf(old, 0.f), block_scale<kInt8>(__uint_as_float(mm)));
             const float inv = inverse_scale(s);
-            plain = plain && s >= 1e-30f;
             unsigned char* rows = a.cache[side] + j * a.kv.head_b + page * a.kv.page_b +
                                   (int64_t)(slot - held) * token_b + 8 * lane;
             // ---- stored rows, where the scale grew
@@ -502,9 +537,13 @@ __global__ void __launch_bounds__(32 * kAppendWarps<T>, append_ctas<T>(H)) appen
                     if (i0 + i < mine)
                         *reinterpret_cast<uint2*>(rows + (i0 + i) * row_step) = encode8<kInt8>(x[i], s, inv);
             }
-            if (kInt8 && !plain) {
-                for (int i = 0; i < mine; ++i)
-                    *reinterpret_cast<uint2*>(rows + i * row_step) = int8_row(x0 + i * step, s, inv);
+            if (!is_plain<kInt8>(finite, s)) {
+                for (int i = 0; i < mine; ++i) {
+                    if constexpr (kInt8)
+                        *reinterpret_cast<uint2*>(rows + i * row_step) = int8_row(x0 + i * step, s, inv);
+                    else
+                        e4m3_codes(rows + i * row_step, x0 + i * step + 8 * lane, s);
+                }
             }
             // the unit's warps have all read the old scale before the barrier above
             if (active && w == 0 && lane == 0)
@@ -611,8 +650,12 @@ __global__ void __launch_bounds__(kRowThreads, U > 1 ? 5 : 8) append_rows_kernel
         const float s = fmaxf(fmaxf(old[u], 0.f), block_scale<kInt8>(__uint_as_float(m)));
         const float inv = inverse_scale(s);
         unsigned char* to = a.cache[side] + j * a.kv.head_b + page * a.kv.page_b + slot * a.kv.token_b + 8 * lane;
-        *reinterpret_cast<uint2*>(to) = kInt8 && !(finite && s >= 1e-30f) ? int8_codes(x[u], s, inv)
-                                                                          : encode8<kInt8>(x[u], s, inv);
+        if (is_plain<kInt8>(finite, s))
+            *reinterpret_cast<uint2*>(to) = encode8<kInt8>(x[u], s, inv);
+        else if constexpr (kInt8)
+            *reinterpret_cast<uint2*>(to) = int8_codes(x[u], s, inv);
+        else
+            e4m3_codes(to, static_cast<const T*>(a.src[side]) + row * a.ts[side] + j * a.hs[side] + 8 * lane, s);
         if (held > 0 && s != old[u])
             recode_rows<kInt8>(to - held * a.kv.token_b, a.kv.token_b, held, old[u], s, inv);
         __syncwarp();                                    // every lane has read the old scale

@@ -6,8 +6,8 @@
 // quotient by a power of two is exact; for INT8 the nearest integer of x inv,
 // inv ~ 1 / s, is corrected by the exact remainder x - q s (encode8).  A block
 // that holds rows already keeps the larger of the two scales and codes those rows
-// again when it grew.  A stored scale may be smaller than any made here: units for
-// which that arithmetic is not exact take a longer way.
+// again when it grew.  A stored scale may be smaller than any made here, or for E4M3 no
+// power of two: units for which that arithmetic is not exact take a longer way.
 //
 // Bound: HBM, each source row read once and its codes written once (8190 rows x 4
 // heads x K and V: 6.4 us; it takes 15.4 us for E4M3 in blocks of 64, 18.3 us for
@@ -233,12 +233,12 @@ __device__ __forceinline__ void e4m3_codes(unsigned char* to, const T* x, float 
 }
 
 // Whether encode8 codes a unit right whose new elements are finite or not and whose
-// scale is s: INT8 where s, s / 2 and 1 / s are far from the subnormals, E4M3 where
-// 1 / s is finite.
+// scale is s: INT8 where s, s / 2 and 1 / s are far from the subnormals, E4M3 where s is
+// 0 or a normal power of two, so that x inv is the quotient.
 template <bool kInt8>
 __device__ __forceinline__ bool is_plain(bool finite, float s)
 {
-    return kInt8 ? finite && s >= 1e-30f : s >= FLT_MIN || s == 0.f;
+    return kInt8 ? finite && s >= 1e-30f : (__float_as_uint(s) & 0x7FFFFFu) == 0u;
 }
 
 // A lane's 8 codes of a plain unit's elements.  INT8: adding 1.5 2^23

@@ -56,3 +56,37 @@ def test_tiny_stored_scales(kind, dtype, step):
         for t in c.kv:
             new = t[torch.from_numpy(c.table[:, 0]).long().cuda(), 5:6 if step else 8]
             assert not bool(((new & 127) == 127).any())
+
+
+def _midpoints(kind):
+    """The midpoints of neighbouring codes and the float32 numbers next to them, of both signs."""
+    values = R._E4M3 if kind == "e4m3" else np.arange(128.0)
+    mid = (values[1:] + values[:-1]) / 2
+    return np.concatenate([mid, -mid])
+
+
+@pytest.mark.parametrize("step", [True, False])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+def test_stored_scales_that_are_no_powers_of_two(kind, dtype, step):
+    """Quotients at and next to every midpoint of the codes, under scales such as amax / 448."""
+    import torch
+    scales = np.concatenate([[0.1, 1 / 3, 0.7, 1.1, 3.0 / 448, 2.0 ** -6 * 1.5, np.nextafter(np.float32(0.25), np.float32(1)),
+                              np.nextafter(np.float32(0.25), np.float32(0))],
+                             np.random.default_rng(1).uniform(0.001, 2, 24)]).astype(np.float32)
+    c = _begun(scales, kind, dtype, step, Hkv=1)
+    t = getattr(torch, dtype)
+    mid = _midpoints(kind)
+    n = 1 if step else 3
+    for x in c.rows:
+        for b, s in enumerate(scales):
+            v = torch.from_numpy(mid * float(s)).to(t)           # the nearest, or the one before or after it
+            if dtype == "float32":
+                v = torch.cat([v, torch.nextafter(v, torch.zeros_like(v)), torch.nextafter(v, 2 * v)])
+            v = v[torch.randperm(v.numel(), generator=torch.Generator().manual_seed(b))][:n * D]
+            x.view(-1)[b * n * D:b * n * D + v.numel()] = v.cuda()
+    for i in (0, 1):                                             # no row's largest outgrows its stored scale
+        top = 448 if kind == "e4m3" else 127
+        limit = torch.from_numpy(np.repeat(scales, n) * np.float32(top) * 0.999).cuda()[:, None, None]
+        c.rows[i].copy_(torch.minimum(torch.maximum(c.rows[i].float(), -limit), limit).to(t))
+    _check(c, step)

@@ -186,11 +186,14 @@ __device__ __forceinline__ uint32_t int8_code(float x, float s, float inv)
     return (uint32_t)(int)fminf(fmaxf(q, -127.f), 127.f) & 0xFFu;
 }
 
-// x / s (s > 0, |x| <= 448 s or infinite or NaN) rounded to odd, so that the rounding
-// to E4M3 is the exact quotient's.  s = m 2^e and x 2^-e, of which no bit that could
-// matter is lost, take the division's remainder away from the subnormals.
+// x / s (|x| <= 448 s or infinite or NaN) rounded to odd, so that the rounding to E4M3
+// is the exact quotient's; 0 where s = 0, but for NaN.  s = m 2^e and x 2^-e, of which
+// no bit that could matter is lost, take the division's remainder away from the
+// subnormals.
 __device__ __forceinline__ float quotient_odd(float x, float s)
 {
+    if (s == 0.f && x == x)
+        return copysignf(0.f, x);
     if (!(fabsf(x) <= FLT_MAX))
         return x;
     int e;
@@ -234,11 +237,11 @@ __device__ __forceinline__ void e4m3_codes(unsigned char* to, const T* x, float 
 
 // Whether encode8 codes a unit right whose new elements are finite or not and whose
 // scale is s: INT8 where s, s / 2 and 1 / s are far from the subnormals, E4M3 where s is
-// 0 or a normal power of two, so that x inv is the quotient.
+// a normal power of two, so that x inv is the quotient, or 0 with elements of 0.
 template <bool kInt8>
 __device__ __forceinline__ bool is_plain(bool finite, float s)
 {
-    return kInt8 ? finite && s >= 1e-30f : (__float_as_uint(s) & 0x7FFFFFu) == 0u;
+    return kInt8 ? finite && s >= 1e-30f : (__float_as_uint(s) & 0x7FFFFFu) == 0u && (finite || s > 0.f);
 }
 
 // A lane's 8 codes of a plain unit's elements.  INT8: adding 1.5 2^23

@@ -131,8 +131,8 @@ int paged_gqa_rope_frequencies(double* inv_freq, int rot_dim, double base, int s
  *     code   = round to nearest even of x / s (0 where s = 0)
  * and where s > s_old the block's stored rows are coded again,
  * code' = round to nearest even of code * s_old / s.  Quotients are rounded
- * once.  Infinities saturate, NaN becomes the E4M3 NaN or INT8 0; both are
- * flagged and do not count for m (PAGED_GQA_FLAG_BAD_VALUE).  A stored scale
+ * once.  Infinities saturate (0 where s = 0), NaN becomes the E4M3 NaN or INT8 0;
+ * both are flagged and do not count for m (PAGED_GQA_FLAG_BAD_VALUE).  A stored scale
  * that is negative, infinite or NaN counts as 0, its rows as zeros (same flag).
  * Appending the same rows at the same positions again changes nothing.
  *

@@ -90,3 +90,39 @@ def test_stored_scales_that_are_no_powers_of_two(kind, dtype, step):
         limit = torch.from_numpy(np.repeat(scales, n) * np.float32(top) * 0.999).cuda()[:, None, None]
         c.rows[i].copy_(torch.minimum(torch.maximum(c.rows[i].float(), -limit), limit).to(t))
     _check(c, step)
+
+
+@pytest.mark.parametrize("route", ["step", "ragged", "single"])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+def test_infinities_in_blocks_of_zeros(kind, dtype, route):
+    """Nothing finite but zeros: the scale is 0, and so is every code but those of NaN; flagged."""
+    import torch
+    block = 1 if route == "single" else 16
+    c = Case([0] * 6, [1] * 6 if route == "step" else [5] * 6, kind=kind, dtype=dtype, block=block, seed=40)
+    n = 1 if route == "step" else 5
+    inf, nan = float("inf"), float("nan")
+    for x in c.rows:
+        x.zero_()
+        x[0::n, 0, 3], x[0::n, 1, 255], x[0::n, 1, 254] = inf, -inf, -0.0
+        x[2 * n, 1, 9] = nan
+        x[3 * n:4 * n] = 0
+        x[4 * n, 0, 8], x[4 * n, 1, 8] = 3.0, -2.0               # a block with a scale: infinities saturate
+    assert c.run(plain=route == "step") == R.BAD_VALUE
+    for t, s, x in zip(c.kv, c.sc, c.rows):
+        t, s, x = t.cpu().numpy(), s.cpu().numpy(), x.double().cpu().numpy()
+        for b in range(6):
+            p = c.table[b, 0]
+            got, new = t[p, :n], x[b * n:(b + 1) * n]
+            scale = s[p, :n] if block == 1 else np.broadcast_to(s[p, 0], (n, 2))
+            zero = scale == 0
+            m = np.abs(np.where(np.isfinite(new), new, 0)).max(-1)
+            assert np.array_equal(zero, (m if block == 1 else np.broadcast_to(m.max(0), m.shape)) == 0)
+            if kind == "int8":
+                want = R.encode(np.where(zero[..., None], np.where(np.isnan(new), np.nan, 0),
+                                         new / np.where(zero, 1, scale)[..., None].astype(np.float64)), kind)
+                assert np.array_equal(got, want)
+            else:
+                assert np.array_equal((got & 127) == 127, np.isnan(new))
+                assert np.all((got & 127)[zero[..., None] & ~np.isnan(new)] == 0)
+                assert np.all((got & 127)[~zero[..., None] & np.isinf(new)] == 126)

@@ -358,6 +358,10 @@ template <bool kInt8>
 __device__ __forceinline__ void recode_rows(unsigned char* row, int64_t step, int n, float old, float s, float inv)
 {
     const bool small = kInt8 && (s < 1e-30f || old < 1e-30f);
+    if (!kInt8 && old < 0x1p-60f) {                      // code * old and its error stay normal numbers
+        old *= 0x1p64f;
+        inv *= 0x1p-64f;
+    }
     uint2 next = n > 0 ? *reinterpret_cast<uint2*>(row) : make_uint2(0u, 0u);
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {

@@ -126,3 +126,32 @@ def test_infinities_in_blocks_of_zeros(kind, dtype, route):
                 assert np.array_equal((got & 127) == 127, np.isnan(new))
                 assert np.all((got & 127)[zero[..., None] & ~np.isnan(new)] == 0)
                 assert np.all((got & 127)[~zero[..., None] & np.isinf(new)] == 126)
+
+
+@pytest.mark.parametrize("route", ["step", "ragged"])
+def test_e4m3_rows_of_subnormal_scales_coded_again(route):
+    """code * s_old at and next to every midpoint of the new codes, below float32's normal numbers."""
+    import torch
+    values, rng = R._E4M3, np.random.default_rng(2)
+    mid = (values[1:] + values[:-1]) / 2
+    olds, codes = [], []
+    for m in mid:                                                # code * k 2^-149 / 2^-126 next to the midpoint
+        for i in rng.choice(np.arange(1, 127), 12, replace=False):
+            k = int(round(m / values[i] * 2.0 ** 23)) + int(rng.integers(-1, 2))
+            if 0 < k < 1 << 23:
+                olds.append(k * 2.0 ** -149)
+                codes.append(i)
+    olds += [2.0 ** -e for e in (60, 61, 100, 118, 126, 149)] + [1.3 * 2.0 ** -59, 1e-30, 3e-36]
+    codes += [7] * 9
+    step = route == "step"
+    c = _begun(olds, "e4m3", "float32", step, Hkv=1)
+    n = 1 if step else 3
+    for x, t in zip(c.rows, c.kv):
+        x[:] = (x.double() * 2.0 ** -127).float()                # the new scale: 2^-126
+        x[-9 * n:] = 1.0                                         # and 2^-8
+        pages = torch.from_numpy(c.table[:, 0]).long().cuda()
+        held = t[pages, :5]
+        held[..., ::2] = torch.tensor(codes, dtype=torch.uint8, device="cuda")[:, None, None, None]
+        held[..., 1::2] = held[..., ::2] | 128
+        t[pages, :5] = held
+    _check(c, step)

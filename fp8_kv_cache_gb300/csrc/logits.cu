@@ -8,8 +8,9 @@
 // has a bias and more than one.  Integer atomics only, so the order of the
 // counts does not matter.  The first logits, the first history entries and the
 // biases are all loaded before anything waits for one of them.  A column with
-// a bias is finished by the thread of its (first) bias entry, which sums the
-// token's entries in their order; the column's own thread leaves it out.
+// a bias is finished by the thread of its bias entry, and one with several by the
+// thread of the column, which sums the token's entries in their order; the stream
+// leaves them out.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -162,36 +163,43 @@ __global__ void __launch_bounds__(kLogitThreads) logits_kernel(LogitsArgs a)
                 count(i0 + i * kLogitThreads, h[i]);
         }
     }
+    int several = 0;                                     // a token with more than one bias
     for (int i = tid; i < n_bias; i += kLogitThreads) {
         const int t = i == tid ? bias_t : __ldg(bt + i);
         if (t >= a.V)
             flags |= PAGED_GQA_FLAG_BAD_INDEX;
-        else if (t >= lo && t < lo + n && (atomicOr(&cnt[t - lo], kBias) & kBias))
+        else if (t >= lo && t < lo + n && (atomicOr(&cnt[t - lo], kBias) & kBias)) {
             atomicOr(&cnt[t - lo], kBiases);
+            several = 1;
+        }
     }
     if (table)
-        __syncthreads();
+        several = __syncthreads_or(several);
 
     // ---- columns with a bias
+    auto finish = [&](int c, float e, uint32_t w, float sum) {
+        const int t = lo + c;
+        const bool ok = mask == nullptr || ((__ldg(mask + (t >> 5)) >> (t & 31)) & 1u);
+        out[c] = ok ? penalised(e, w, p) + sum : -INFINITY;
+    };
     for (int i = tid; i < n_bias; i += kLogitThreads) {
         const int t = i == tid ? bias_t : __ldg(bt + i);
         if (t < lo || t >= lo + n)
             continue;
         const uint32_t w = cnt[t - lo];
-        float sum = i == tid ? bias_v : __ldg(bv + i);
-        if (w & kBiases) {
-            bool first = true;
-            for (int k = 0; k < i && first; ++k)
-                first = __ldg(bt + k) != t;
-            if (!first)
-                continue;
-            for (int k = i + 1; k < n_bias; ++k)
-                if (__ldg(bt + k) == t)
-                    sum += __ldg(bv + k);
-        }
-        const float e = i == tid ? bias_x : (float)x[t - lo];
-        const bool ok = mask == nullptr || ((__ldg(mask + (t >> 5)) >> (t & 31)) & 1u);
-        out[t - lo] = ok ? penalised(e, w, p) + sum : -INFINITY;
+        if (!(w & kBiases))
+            finish(t - lo, i == tid ? bias_x : (float)x[t - lo], w, i == tid ? bias_v : __ldg(bv + i));
+    }
+    // those with several: one sweep over the entries for each (a thread to every entry,
+    // looking for the token's first one, takes the square of n_bias)
+    for (int c = several ? tid : n; c < n; c += kLogitThreads) {
+        if (!(cnt[c] & kBiases))
+            continue;
+        float sum = -0.f;                                // adds nothing
+        for (int i = 0; i < n_bias; ++i)
+            if (__ldg(bt + i) == lo + c)
+                sum += __ldg(bv + i);
+        finish(c, (float)x[c], cnt[c], sum);
     }
 
     // ---- the others: penalties and mask

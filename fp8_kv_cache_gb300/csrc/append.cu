@@ -64,7 +64,7 @@ struct Row {
     {
 #pragma unroll
         for (int i = 0; i < kParts; ++i)
-            w[i] = __ldg(reinterpret_cast<const uint4*>(row) + kParts * lane + i);
+            w[i] = reinterpret_cast<const uint4*>(row)[kParts * lane + i];
     }
     __device__ void clear()
     {
@@ -385,7 +385,7 @@ __device__ __forceinline__ int sequence_of(const AppendArgs& a, int row, int* fo
         *found = -1;
     __syncthreads();
     for (int i = threadIdx.x; i < a.B; i += blockDim.x) {
-        const int o = __ldg(a.offs + i), o1 = __ldg(a.offs + i + 1);
+        const int o = a.offs[i], o1 = a.offs[i + 1];
         asm volatile("prefetch.global.L1 [%0];" ::"l"(a.starts + i));
         if (o <= row && row < o1)
             atomicMax(found, i);
@@ -443,16 +443,16 @@ __global__ void __launch_bounds__(32 * kAppendWarps<T>, append_ctas<T>(H)) appen
             b = sequence_of(a, (int)row, &found);
             if (b < 0) {
                 // in front of the first sequence, or behind the last one
-                const int o = __ldg(a.offs);
+                const int o = a.offs[0];
                 if (o <= row)
                     break;
                 row = o;
                 continue;
             }
-            off = max(__ldg(a.offs + b), 0);
-            end = min(__ldg(a.offs + b + 1), a.T);
+            off = max(a.offs[b], 0);
+            end = min(a.offs[b + 1], a.T);
         }
-        const int start = __ldg(a.starts + b);
+        const int start = a.starts[b];
         if (start < 0) {
             flags |= PAGED_GQA_FLAG_EMPTY_ROW;
             row = end;
@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps<T>, append_ctas<T>(H)) appen
                 for (int i = 0; i < H; ++i)
                     x[i].top(m);
             }
-            const int page = table_page(a.kv, a.bt + b * a.bt_stride, pi, flags);
+            const int page = table_page<false>(a.kv, a.bt + b * a.bt_stride, pi, flags);
             if (page < 0)
                 continue;                                // every warp has the same page
             float* scale = a.scales[side] + page * a.sc.page + sb * a.sc.block_stride + j * a.sc.head;
@@ -592,16 +592,16 @@ __global__ void __launch_bounds__(kRowThreads, U > 1 ? 5 : 8) append_rows_kernel
     if (a.offs != nullptr) {
         b = -1;
         for (int i = lane; i < a.B; i += 32) {
-            const int o = __ldg(a.offs + i), o1 = __ldg(a.offs + i + 1);
+            const int o = a.offs[i], o1 = a.offs[i + 1];
             asm volatile("prefetch.global.L1 [%0];" ::"l"(a.starts + i));
             b = o <= row && row < o1 ? i : b;
         }
         b = __reduce_max_sync(0xffffffffu, b);
         if (b < 0)
             return;                                      // no sequence's
-        off = max(__ldg(a.offs + b), 0);
+        off = max(a.offs[b], 0);
     }
-    const int start = __ldg(a.starts + b);
+    const int start = a.starts[b];
     const bool past = row >= off + a.max_len - start;
     int page = -1, slot = 0;
     if (start < 0) {
@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(kRowThreads, U > 1 ? 5 : 8) append_rows_kernel
     } else {
         int pi;
         page_and_slot(a.kv, start + (int)(row - off), pi, slot);
-        page = table_page(a.kv, a.bt + b * a.bt_stride, pi, flags);
+        page = table_page<false>(a.kv, a.bt + b * a.bt_stride, pi, flags);
     }
     if (page < 0) {
         raise_flag(a.err, flags);

@@ -33,7 +33,7 @@ using scaled::Smem;
 
 __device__ __forceinline__ int length_of(const ScaledDecodeArgs& a, int b)
 {
-    return min(max(__ldg(a.seq_lens + b), 0), a.max_seq_len);
+    return min(max(a.seq_lens[b], 0), a.max_seq_len);
 }
 
 // Tiles of sequence b on the line, the piece cost included (0: empty).
@@ -71,7 +71,7 @@ __device__ __forceinline__ void run_piece(const ScaledDecodeArgs& a, const Smem<
         if (t < L) {
             int pi, slot;
             page_and_slot(a.c.kv, t, pi, slot);
-            const int page = table_page(a.c.kv, bt_row, pi, flags);
+            const int page = table_page<false>(a.c.kv, bt_row, pi, flags);
             if (page >= 0)
                 return scaled::place_of(a.c, page, slot, j);
         }
@@ -95,7 +95,7 @@ __device__ __forceinline__ float* group_slots(const ScaledDecodeArgs& a, int gro
 // The flags of sequence b's length.
 __device__ __forceinline__ int length_flags(const ScaledDecodeArgs& a, int b)
 {
-    const int raw = __ldg(a.seq_lens + b);
+    const int raw = a.seq_lens[b];
     return (raw > a.max_seq_len ? PAGED_GQA_FLAG_SEQ_CLAMPED : 0) | (raw <= 0 ? PAGED_GQA_FLAG_EMPTY_ROW : 0);
 }
 

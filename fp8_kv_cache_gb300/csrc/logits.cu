@@ -106,26 +106,26 @@ __global__ void __launch_bounds__(kLogitThreads) logits_kernel(LogitsArgs a)
     if (hist != nullptr) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
-            h[i] = tid + i * kLogitThreads < r.max_history ? __ldg(hist + tid + i * kLogitThreads) : -1;
-        len = r.history_lens != nullptr ? min(max(__ldg(r.history_lens + b), 0), r.max_history)
+            h[i] = tid + i * kLogitThreads < r.max_history ? hist[tid + i * kLogitThreads] : -1;
+        len = r.history_lens != nullptr ? min(max(r.history_lens[b], 0), r.max_history)
                                         : r.max_history;
-        prompt = r.prompt_lens != nullptr ? __ldg(r.prompt_lens + b) : 0;
-        p.repetition = r.repetition != nullptr ? __ldg(r.repetition + b) : 1.f;
-        p.frequency = r.frequency != nullptr ? __ldg(r.frequency + b) : 0.f;
-        p.presence = r.presence != nullptr ? __ldg(r.presence + b) : 0.f;
+        prompt = r.prompt_lens != nullptr ? r.prompt_lens[b] : 0;
+        p.repetition = r.repetition != nullptr ? r.repetition[b] : 1.f;
+        p.frequency = r.frequency != nullptr ? r.frequency[b] : 0.f;
+        p.presence = r.presence != nullptr ? r.presence[b] : 0.f;
     }
     const int32_t* bt = r.bias_tokens != nullptr ? r.bias_tokens + b * r.bias_stride : nullptr;
     const float* bv = bt != nullptr ? r.bias_values + b * r.bias_stride : nullptr;
     const int n_bias = bt != nullptr ? r.n_bias : 0;
-    int bias_t = tid < n_bias ? __ldg(bt + tid) : -1;    // the thread's first bias entry
+    int bias_t = tid < n_bias ? bt[tid] : -1;        // the thread's first bias entry
     float bias_x = 0.f, bias_v = 0.f;
     if (bias_t >= lo && bias_t < lo + n) {
-        bias_v = __ldg(bv + tid);
+        bias_v = bv[tid];
         bias_x = (float)x[bias_t - lo];
     }
     const uint32_t* mask = nullptr;
     if (r.mask != nullptr) {
-        const int m = r.mask_index != nullptr ? __ldg(r.mask_index + b) : b;
+        const int m = r.mask_index != nullptr ? r.mask_index[b] : b;
         if (m >= r.mask_rows)
             flags |= PAGED_GQA_FLAG_BAD_INDEX;
         else if (m >= 0)
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kLogitThreads) logits_kernel(LogitsArgs a)
         for (int i0 = tid + kAhead * kLogitThreads; i0 < len; i0 += kAhead * kLogitThreads) {
 #pragma unroll
             for (int i = 0; i < kAhead; ++i)
-                h[i] = i0 + i * kLogitThreads < len ? __ldg(hist + i0 + i * kLogitThreads) : -1;
+                h[i] = i0 + i * kLogitThreads < len ? hist[i0 + i * kLogitThreads] : -1;
 #pragma unroll
             for (int i = 0; i < kAhead; ++i)
                 count(i0 + i * kLogitThreads, h[i]);
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kLogitThreads) logits_kernel(LogitsArgs a)
     }
     int several = 0;                                     // a token with more than one bias
     for (int i = tid; i < n_bias; i += kLogitThreads) {
-        const int t = i == tid ? bias_t : __ldg(bt + i);
+        const int t = i == tid ? bias_t : bt[i];
         if (t >= a.V)
             flags |= PAGED_GQA_FLAG_BAD_INDEX;
         else if (t >= lo && t < lo + n && (atomicOr(&cnt[t - lo], kBias) & kBias)) {
@@ -179,16 +179,16 @@ __global__ void __launch_bounds__(kLogitThreads) logits_kernel(LogitsArgs a)
     // ---- columns with a bias
     auto finish = [&](int c, float e, uint32_t w, float sum) {
         const int t = lo + c;
-        const bool ok = mask == nullptr || ((__ldg(mask + (t >> 5)) >> (t & 31)) & 1u);
+        const bool ok = mask == nullptr || ((mask[t >> 5] >> (t & 31)) & 1u);
         out[c] = ok ? penalised(e, w, p) + sum : -INFINITY;
     };
     for (int i = tid; i < n_bias; i += kLogitThreads) {
-        const int t = i == tid ? bias_t : __ldg(bt + i);
+        const int t = i == tid ? bias_t : bt[i];
         if (t < lo || t >= lo + n)
             continue;
         const uint32_t w = cnt[t - lo];
         if (!(w & kBiases))
-            finish(t - lo, i == tid ? bias_x : (float)x[t - lo], w, i == tid ? bias_v : __ldg(bv + i));
+            finish(t - lo, i == tid ? bias_x : (float)x[t - lo], w, i == tid ? bias_v : bv[i]);
     }
     // those with several: one sweep over the entries for each (a thread to every entry,
     // looking for the token's first one, takes the square of n_bias)
@@ -197,8 +197,8 @@ __global__ void __launch_bounds__(kLogitThreads) logits_kernel(LogitsArgs a)
             continue;
         float sum = -0.f;                                // adds nothing
         for (int i = 0; i < n_bias; ++i)
-            if (__ldg(bt + i) == lo + c)
-                sum += __ldg(bv + i);
+            if (bt[i] == lo + c)
+                sum += bv[i];
         finish(c, (float)x[c], cnt[c], sum);
     }
 
@@ -206,6 +206,12 @@ __global__ void __launch_bounds__(kLogitThreads) logits_kernel(LogitsArgs a)
     for (int c0 = 0; c0 < n; c0 += kWindow) {
         if (c0 > 0)
             load(c0);
+        uint32_t bits[N];                                // ahead of the stores
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            const int c = c0 + 4 * (tid + u * kLogitThreads);
+            bits[u] = mask != nullptr && c < n ? mask[(lo + c) >> 5] >> (c & 31) : 0u;
+        }
 #pragma unroll
         for (int u = 0; u < N; ++u) {
             const int c = c0 + 4 * (tid + u * kLogitThreads);
@@ -227,10 +233,9 @@ __global__ void __launch_bounds__(kLogitThreads) logits_kernel(LogitsArgs a)
                 }
             }
             if (mask != nullptr) {
-                const uint32_t bits = __ldg(mask + ((lo + c) >> 5)) >> (c & 31);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (!((bits >> i) & 1u))
+                    if (!((bits[u] >> i) & 1u))
                         e[i] = -INFINITY;
             }
             if (vec && c + 4 <= n && skip == 0u) {

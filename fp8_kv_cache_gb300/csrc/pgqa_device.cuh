@@ -130,12 +130,25 @@ __device__ __forceinline__ void page_and_slot(const KVGeom& g, int t, int& pi, i
     }
 }
 
+// *p.  kStable: no kernel that may still run when this one starts writes it, so that
+// the read-only path is allowed; otherwise an ordinary load, which what orders the two
+// kernels orders, too.
+template <bool kStable, class T>
+__device__ __forceinline__ T load(const T* p)
+{
+    if constexpr (kStable)
+        return __ldg(p);
+    else
+        return *p;
+}
+
 // Physical page named by entry pi of the block-table row bt_row, or -1 when it
 // is outside [0, num_pages) (then PAGED_GQA_FLAG_BAD_PAGE is added to flags).
+template <bool kStable = true>
 __device__ __forceinline__ int table_page(const KVGeom& g, const int32_t* bt_row, int pi,
                                           int& flags)
 {
-    const int page = __ldg(bt_row + pi);
+    const int page = load<kStable>(bt_row + pi);
     if (page < 0 || page >= g.num_pages) {
         flags |= PAGED_GQA_FLAG_BAD_PAGE;
         return -1;
@@ -166,6 +179,7 @@ __device__ __forceinline__ int64_t token_row_offset(const KVGeom& g, const int32
 // the entry is not attended: padding, a block not strictly before the row's
 // own block (PAGED_GQA_FLAG_BAD_SEL), or an invalid page id).  A block never
 // straddles pages because page_size is a multiple of 4.
+template <bool kStable = true>
 __device__ __forceinline__ void prefill_entry(const KVGeom& g, const int32_t* bt,
                                               const int32_t* sel_row, int n_sel, int own, int e,
                                               int& first, int& page, int& flags)
@@ -173,7 +187,7 @@ __device__ __forceinline__ void prefill_entry(const KVGeom& g, const int32_t* bt
     page = -1;
     first = 0;
     if (e < n_sel) {
-        const int b = __ldg(sel_row + e);
+        const int b = load<kStable>(sel_row + e);
         if (b < 0)
             return;                           // padding
         if (b >= own) {
@@ -188,7 +202,7 @@ __device__ __forceinline__ void prefill_entry(const KVGeom& g, const int32_t* bt
     }
     int pi, slot;
     page_and_slot(g, first, pi, slot);
-    page = table_page(g, bt, pi, flags);
+    page = table_page<kStable>(g, bt, pi, flags);
 }
 
 // Whether lane u (0..3) of entry e is attended, given its page: every token

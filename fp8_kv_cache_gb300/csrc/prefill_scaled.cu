@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(32 * kNW, kNW > 4 ? 1 : kClusters ? 2 : 3)
     int flags = 0;
     __half* out_rows = a.out + ((size_t)r * a.Hq + (size_t)j * a.G) * kD;
     enter();
-    int p = __ldg(a.q_pos + r);
+    int p = a.q_pos[r];
     const bool empty = p < 0 || a.kv_len <= 0;
     if (empty) {
         flags |= PAGED_GQA_FLAG_EMPTY_ROW;
@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(32 * kNW, kNW > 4 ? 1 : kClusters ? 2 : 3)
         __syncthreads();                             // Q staged, the previous chunk done with tab
         for (int e = e0 + (int)threadIdx.x; e < e1; e += 32 * kNW) {
             int first, page;
-            prefill_entry(a.c.kv, a.bt, sel_row, a.n_sel, own, e, first, page, flags);
+            prefill_entry<false>(a.c.kv, a.bt, sel_row, a.n_sel, own, e, first, page, flags);
             tab[e - e0] = make_int2(first, page);
         }
         __syncthreads();

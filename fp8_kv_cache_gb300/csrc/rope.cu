@@ -173,10 +173,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a, int lane
         load(h + step, u1, v1);
         if (!ready) {
             // the first rows are on their way while the angles are computed
-            const int pos = __ldg(a.pos + t);
+            const int pos = a.pos[t];
 #pragma unroll 4
             for (int p = lane; p < pairs; p += 32) {
-                const float2 r = cos_sin(pos, turns_of(__ldg(a.freq + p)));
+                const float2 r = cos_sin(pos, turns_of(a.freq[p]));
                 c[p] = make_float2(a.scale * r.x, a.inverse ? -a.scale * r.y : a.scale * r.y);
             }
             __syncwarp();
@@ -230,11 +230,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_pairs_kernel(RopeArgs a)
     const int t = blockIdx.x, pairs = a.rot >> 1, items = pairs + a.D - a.rot;
     const int Hq = a.t[0].heads, H = Hq + a.t[1].heads;
     enter();
-    const int pos = __ldg(a.pos + t);
+    const int pos = a.pos[t];
     for (int i = threadIdx.x; i < items; i += kRopeThreads) {
         float2 r = make_float2(0.f, 0.f);
         if (i < pairs) {
-            r = cos_sin(pos, turns_of(__ldg(a.freq + i)));
+            r = cos_sin(pos, turns_of(a.freq[i]));
             r = make_float2(a.scale * r.x, a.inverse ? -a.scale * r.y : a.scale * r.y);
         }
         const int d0 = a.half ? i : 2 * i, d1 = a.half ? i + pairs : 2 * i + 1;

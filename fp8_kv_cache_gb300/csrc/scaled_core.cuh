@@ -170,7 +170,7 @@ __device__ __forceinline__ void stage_q(uint4* qs, const __half* qg, int G, int 
 {
     const int g = lane >> 2, q = lane & 3;
     const uint32_t* row = reinterpret_cast<const uint32_t*>(qg + (size_t)g * kD);
-    auto two = [&](int i) { return __ldg(row + (WarpCore<true>::k_dim(q, i) >> 1)); };
+    auto two = [&](int i) { return row[WarpCore<true>::k_dim(q, i) >> 1]; };
     for (int s = w; s < 8; s += nw)
         qs[s * 32 + lane] = g < G ? make_uint4(two(8 * s), two(8 * s + 2), two(8 * s + 4), two(8 * s + 6))
                                   : make_uint4(0u, 0u, 0u, 0u);

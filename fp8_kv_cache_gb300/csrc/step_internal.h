@@ -15,7 +15,10 @@ namespace pgqa {
 // The step's kernels are launched as programmatic dependents of whatever kernel
 // precedes them on the stream: their CTAs are placed while it drains, and wait in
 // enter() -- before they touch global memory -- until it has completed.  From there
-// on their own successors may be placed.  One token rotated call after call takes
+// on their own successors may be placed.  What they read may have been written by a
+// kernel that was still running when they started, so they read it by ordinary loads and
+// copies, never by the read-only path (__ldg, __restrict__), whose data must not change
+// while a kernel lives, and whose loads need not stay behind the wait.  One token rotated call after call takes
 // 3.05 us a call instead of 4.10, at the same time on the host.
 __device__ __forceinline__ void enter()
 {

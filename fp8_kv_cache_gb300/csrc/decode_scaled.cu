@@ -36,10 +36,16 @@ __device__ __forceinline__ int length_of(const ScaledDecodeArgs& a, int b)
     return min(max(a.seq_lens[b], 0), a.max_seq_len);
 }
 
+// Tiles of n tokens (n + kTile - 1 would pass 31 bits for the longest).
+__device__ __forceinline__ int tiles_of(int n)
+{
+    return n / kTile + (n % kTile != 0);
+}
+
 // Tiles of sequence b on the line, the piece cost included (0: empty).
 __device__ __forceinline__ int64_t line_tiles(const ScaledDecodeArgs& a, int b)
 {
-    const int n = (length_of(a, b) + kTile - 1) / kTile;
+    const int n = tiles_of(length_of(a, b));
     return n > 0 ? n + kSplitPieceTiles : 0;
 }
 
@@ -122,7 +128,7 @@ __global__ void __launch_bounds__(32 * kNW, kNW > 4 ? 1 : 2)
     ClusterJoin join(*reinterpret_cast<Inbox*>(sm.tail), size, rank);
     enter();
     int flags = rank == 0 && tid == 0 ? length_flags(a, b) : 0;
-    const int L = length_of(a, b), n = (L + kTile - 1) / kTile;
+    const int L = length_of(a, b), n = tiles_of(L);
     __half* out_rows = a.out + ((size_t)b * a.Hq + (size_t)j * a.G) * kD;
     const int ta = (int)((int64_t)n * rank / size), te = (int)((int64_t)n * (rank + 1) / size);
     run_piece<kInt8>(a, sm, b, j, L, ta, te, flags,

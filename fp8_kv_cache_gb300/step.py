@@ -347,7 +347,7 @@ def _q_out(q, out, dev, stream, Hkv, D):
     if q.dtype is not _F16:
         raise TypeError(f"q must be torch.float16, not {q.dtype}")
     shape = q.shape
-    if len(shape) != 3 or shape[2] != D or not q.is_contiguous() or shape[1] % Hkv != 0:
+    if len(shape) != 3 or shape[2] != D or not q.is_contiguous() or Hkv < 1 or shape[1] % Hkv != 0:
         raise ValueError("q must be a contiguous [rows, Hq, D] tensor, Hq a multiple of the "
                          "cache's heads")
     if out is None:

@@ -378,7 +378,8 @@ def paged_gqa_decode_scaled(q, k_cache, v_cache, k_scales, v_scales, block_table
     at most max_seq_len (default: all the table covers).  ``workspace``: a
     CUDA uint8 tensor of paged_gqa_decode_scaled_workspace_size bytes, None to
     allocate one, False for none (long contexts are slower without); calls that
-    may overlap need one each.  Returns out."""
+    may overlap need one each.  ``force_splits`` CTAs share all tokens; without
+    effect where there is no workspace, or more than 4096 sequences.  Returns out."""
     dev = q.get_device()
     if not (dev == k_cache.get_device() == v_cache.get_device() == k_scales.get_device() ==
             v_scales.get_device() == block_table.get_device() == seq_lens.get_device() >= 0):

@@ -193,7 +193,8 @@ size_t paged_gqa_decode_scaled_workspace_size(int B, int Hq, int Hkv, int D, int
  *                merge their results in a second kernel, which long contexts
  *                need; it does so where that is the faster way for B, Hkv and
  *                max_seq_len, and always with force_splits.  Otherwise, and
- *                without a workspace, a cluster of up to 8 CTAs takes each
+ *                without a workspace or for a batch above 4096 whatever
+ *                force_splits says, a cluster of up to 8 CTAs takes each
  *                (sequence, KV head) in one kernel.  A workspace shared by two
  *                calls in flight races.
  * Results are deterministic for a given device, shape and workspace choice.

@@ -34,3 +34,25 @@ def test_the_longest_sequence(length):
     want = torch.softmax(q[0].double() @ k.T / 16, -1) @ v
     assert int(err.item()) == 1
     assert bool(((out[0].double() - want).abs() <= want * (2.0 ** -11 + 2.0 ** -13)).all())
+
+
+@pytest.mark.parametrize("B", [3, 4096, 4097])
+def test_forced_splits_where_there_is_no_split(B):
+    """Without a workspace, or for more than 4096 sequences, force_splits changes nothing, not a bit."""
+    import torch
+    import fp8_kv_cache_gb300 as P
+    g = torch.Generator(device="cuda").manual_seed(B)
+    codes = [torch.randint(-127, 128, (64, 16, 1, D), device="cuda", generator=g).to(torch.int8) for _ in (0, 1)]
+    sc = [torch.full((64, 1, 1), 0.01, device="cuda") for _ in (0, 1)]
+    table = torch.randint(0, 64, (B, 4), device="cuda", generator=g).int()
+    lens = torch.randint(0, 65, (B,), device="cuda", generator=g).int()
+    q = torch.randn(B, 2, D, device="cuda", generator=g).half()
+
+    def call(**kw):
+        return P.paged_gqa_decode_scaled(q, *codes, *sc, table, lens, 16, 1 / 16, **kw)
+
+    plain = call(workspace=False)
+    assert torch.equal(call(workspace=False, force_splits=5), plain)
+    forced = call(force_splits=5)
+    assert torch.equal(forced, plain) or B <= 4096
+    assert bool(((forced.double() - plain.double()).abs() <= 2.0 ** -10 * plain.double().abs() + 2.0 ** -24).all())

@@ -166,11 +166,11 @@ int split_ctas(int (&n)[2])
 void choose_cluster(int64_t segments, int64_t tiles, int& cluster, int& warps)
 {
     cluster = 8;
-    while (cluster > 1 && (segments * cluster > 304 || tiles <= 2 * cluster))
+    while (cluster > 1 && (segments * cluster > 2 * kSms || tiles <= 2 * cluster))
         cluster /= 2;
-    if (cluster == 8 && segments * 8 > 112 && segments * 4 <= 152)
+    if (cluster == 8 && segments * 8 > 112 && segments * 4 <= kSms)
         cluster = 4;
-    warps = segments * cluster <= (cluster == 8 ? 112 : 152) && tiles > 4 ? 8 : 4;
+    warps = segments * cluster <= (cluster == 8 ? 112 : kSms) && tiles > 4 ? 8 : 4;
 }
 
 // Whether C split CTAs and a merge kernel beat the clusters: they share all

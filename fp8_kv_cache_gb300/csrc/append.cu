@@ -50,9 +50,9 @@ constexpr int append_ctas(int h)
 {
     return sizeof(T) == 4 ? (h > 4 ? 2 : 3) : h > 8 ? 4 : h > 4 ? 6 : 8;
 }
-constexpr int64_t kAppendCtas = 3 * 152;     // CTAs that keep the GPU busy
+constexpr int64_t kAppendCtas = 3 * kSms;    // CTAs that keep the GPU busy
 constexpr int kRowThreads = 128;
-constexpr int64_t kRowWarps = 64 * 152;      // most of one unit
+constexpr int64_t kRowWarps = 64 * kSms;     // most of one unit
 
 // A lane's 8 elements of a row, as loaded.
 template <class T>

@@ -289,13 +289,13 @@ cudaError_t logits_typed(LogitsArgs a, cudaStream_t s)
         const int64_t w = ((a.V + most - 1) / most * a.B + slots - 1) / slots, k = slots * w / a.B;
         return (int)std::max<int64_t>(((a.V + k - 1) / k + 31) / 32 * 32, 2048);
     };
-    a.cols = share(304, kLogitCols / 2);
+    a.cols = share(2 * kSms, kLogitCols / 2);
     // Every CTA reads its row's whole history: where that is half as long as the
     // share or more, one CTA of 1024 threads per SM in place of two of 512 (32,768
     // tokens 15.5 us and 18.2 us), unless they would have too few columns and a
     // history that half the threads load at once (one row, 4096 tokens: 3.8 and 3.3).
     const int64_t history = a.r.history != nullptr ? a.r.max_history : 0;
-    const int wide = share(152, kLogitCols);
+    const int wide = share(kSms, kLogitCols);
     if (2 * history > a.cols && (wide >= 4096 || history > 8192)) {
         a.cols = wide;
         return logits_run<T, 4, 1024>(a, s);

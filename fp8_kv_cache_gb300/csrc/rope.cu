@@ -285,7 +285,7 @@ cudaError_t rope_run(const RopeArgs& a, cudaStream_t s)
     // each), then fewer with more rows for the same angles (1024 tokens: 5
     // warps each 6.6 us, 10 warps 7.9 us).
     const int64_t steps = (H + 32 / lanes - 1) / (32 / lanes);
-    const int64_t shares = std::clamp<int64_t>((32 * 152 + a.T - 1) / a.T, 1, steps);
+    const int64_t shares = std::clamp<int64_t>((32 * kSms + a.T - 1) / a.T, 1, steps);
     int threads = kRopeThreads;                               // fewer where the pairs are many: 48 KB
     while (threads > 32 && (size_t)(threads / 32) * pairs * sizeof(float2) > 48 * 1024)
         threads /= 2;

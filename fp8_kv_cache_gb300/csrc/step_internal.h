@@ -12,6 +12,12 @@
 
 namespace pgqa {
 
+// SMs of the GPU that this library is built and measured for.  The launch rules count
+// with it; elsewhere they would pick other shapes than the fastest, with the same results
+// but for the order of sums.  (What has to fit the device, the CTAs of the split decode,
+// is asked of the device.)
+constexpr int kSms = 152;
+
 // The step's kernels are launched as programmatic dependents of whatever kernel
 // precedes them on the stream: their CTAs are placed while it drains, and wait in
 // enter() -- before they touch global memory -- until it has completed.  From there
@@ -92,7 +98,7 @@ struct ScaledDecodeArgs {
     float scale_log2;             // softmax_scale * log2(e)
     __half* out;
     // split route only
-    int64_t* hdr;                 // [0] = T, [1] = C_eff, then prefix[B + 1]
+    int64_t* hdr;                 // prefix[B + 1] from [2] on, for batches above kMergeScanMax
     float* slots;                 // C + B * Hkv partial slots
     int C;                        // CTAs launched on the split route; 0: a cluster per segment
     int groups, heads;            // of CTAs, with a line of tiles each; KV heads of a group

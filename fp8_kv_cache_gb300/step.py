@@ -304,8 +304,8 @@ def paged_gqa_append_scaled(k, v, k_cache, v_cache, k_scales, v_scales, block_ta
     tokens stored before).  A scale block that already holds rows keeps the
     larger scale, and its rows are coded again when it grows.  block_table
     int32 [B, pages]; rows at positions from max_seq_len (default: all the
-    table covers) on are dropped.  No page may be written for two sequences in
-    one call.  Returns (k_cache, v_cache)."""
+    table covers) on are dropped.  No page may be written for two sequences, or
+    in two places of one, in a call.  Returns (k_cache, v_cache)."""
     kind = _FLOAT.get(k.dtype)
     if kind is None or v.dtype is not k.dtype:
         raise TypeError("k and v must both be float16, bfloat16 or float32")

@@ -152,8 +152,8 @@ int paged_gqa_rope_frequencies(double* inv_freq, int rot_dim, double base, int s
  *  max_seq_len    rows at positions from here on are dropped
  *                 (PAGED_GQA_FLAG_SEQ_CLAMPED), rows on pages outside the
  *                 pool too (PAGED_GQA_FLAG_BAD_PAGE).
- * The pages written must belong to one sequence each: rows two sequences
- * write to one block race.  Results are deterministic.  One kernel is
+ * The pages written must belong to one sequence each, and to one place of its
+ * table row: rows written to one block from two places race.  Results are deterministic.  One kernel is
  * launched; no workspace.
  */
 int paged_gqa_append_scaled(const void* k, int64_t k_token_stride, int64_t k_head_stride,
@@ -225,12 +225,12 @@ int paged_gqa_sparse_prefill_scaled(const void* q, const void* k_cache, const vo
 /* ------------------------------------------------------------ logits */
 
 /* What changes a step's logits; every part is optional (NULL pointers).
- *  history        device int32, row b at history + b * history_stride: the
- *                 token ids of sequence b so far, history_lens[b] of them
- *                 (device int32 [B], clamped to 0 .. max_history; NULL:
- *                 max_history).  Negative ids are padding.  The first
- *                 prompt_lens[b] (NULL: 0) are the prompt's, the others were
- *                 generated.
+ *  history        device int32, row b of max_history entries at history +
+ *                 b * history_stride: the token ids of sequence b so far,
+ *                 history_lens[b] of them (device int32 [B], clamped to 0 ..
+ *                 max_history; NULL: max_history).  Negative ids are padding.
+ *                 The first prompt_lens[b] (NULL: 0) are the prompt's, the
+ *                 others were generated.
  *  repetition     device float32 [B], > 0: logits of all tokens in the history
  *                 are divided by it where positive and multiplied where not.
  *  frequency,     device float32 [B]: logits lose frequency * count + presence

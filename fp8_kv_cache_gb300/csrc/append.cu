@@ -353,11 +353,12 @@ __device__ __forceinline__ uint2 recode8(uint2 w, float old, float s, float inv)
 }
 
 // A lane's codes of n rows `step` bytes apart, coded again; the next row is loaded
-// ahead.
+// ahead.  old: negative where the stored scale was none.
 template <bool kInt8>
 __device__ __forceinline__ void recode_rows(unsigned char* row, int64_t step, int n, float old, float s, float inv)
 {
     const bool small = kInt8 && (s < 1e-30f || old < 1e-30f);
+    const bool zeros = kInt8 ? !(old > 0.f) : old < 0.f;     // E4M3 keeps its NaN under a scale of 0
     if (!kInt8 && old < 0x1p-60f) {                      // code * old and its error stay normal numbers
         old *= 0x1p64f;
         inv *= 0x1p-64f;
@@ -370,9 +371,7 @@ __device__ __forceinline__ void recode_rows(unsigned char* row, int64_t step, in
         row += step;
         if (i + 1 < n)
             next = *reinterpret_cast<uint2*>(row);
-        *at = !(old > 0.f) ? make_uint2(0u, 0u)
-              : small      ? int8_recode_small(now, old, s)
-                           : recode8<kInt8>(now, old, s, inv);
+        *at = zeros ? make_uint2(0u, 0u) : small ? int8_recode_small(now, old, s) : recode8<kInt8>(now, old, s, inv);
     }
 }
 

@@ -155,3 +155,19 @@ def test_e4m3_rows_of_subnormal_scales_coded_again(route):
         held[..., 1::2] = held[..., ::2] | 128
         t[pages, :5] = held
     _check(c, step)
+
+
+@pytest.mark.parametrize("step", [True, False])
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+def test_scales_that_grow_from_zero(kind, step):
+    """Rows stored under a scale of 0 are code * 0 / s: zeros of their signs, and NaN stays NaN."""
+    import torch
+    c = _begun(np.zeros(20, np.float32), kind, "float16", step, Hkv=2)
+    if kind == "e4m3":
+        for t in c.kv:
+            t[torch.from_numpy(c.table[::2, 0]).long().cuda(), 3, 1, ::9] = 0x7F
+    _check(c, step)
+    if kind == "e4m3":
+        for t, s in zip(c.kv, c.sc):
+            got = t.cpu().numpy()[c.table[::2, 0], 3, 1]
+            assert np.all((got & 127)[:, ::9] == 127) and np.all(s.cpu().numpy()[c.table[:, 0], 0] > 0)

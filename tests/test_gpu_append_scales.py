@@ -171,3 +171,39 @@ def test_scales_that_grow_from_zero(kind, step):
         for t, s in zip(c.kv, c.sc):
             got = t.cpu().numpy()[c.table[::2, 0], 3, 1]
             assert np.all((got & 127)[:, ::9] == 127) and np.all(s.cpu().numpy()[c.table[:, 0], 0] > 0)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("block,B,rows", [(16, 3300, 1), (1, 40, 90), (3, 20, 7), (8, 20, 11), (32, 12, 40),
+                                          (64, 12, 70), (392, 6, 500)])
+def test_every_route(block, B, rows, kind, dtype):
+    """Odd stored scales, zeros and infinities where warps take one unit or several, and where one, two or
+    more warps share a unit of few or many rows."""
+    import torch
+    page = 784 if block == 392 else 48 if block == 3 else 64 if block > 16 else 16
+    start = min(2, block - 1)
+    c = Case([start] * B, [rows] * B, Hkv=3, kind=kind, dtype=dtype, page=page, block=block, seed=block)
+    odd = np.float32([0.1, 2.0 ** -140, 1.1, 0.0, 2.0 ** -6, 3e-39, 1 / 3, 2.0 ** -126])
+    pages = torch.from_numpy(c.table[:, 0]).long().cuda()
+    for s in c.sc:
+        s[pages, 0] = torch.from_numpy(np.resize(odd, (B, 3))).cuda()
+    given = []
+    for x in c.rows:
+        v = x.view(B, rows, 3, D)
+        v[::3, :, 0], v[1::3, :, 1], v[2::3, :, 2] = 0, 0, -0.0
+        v[::5] *= 40
+        v[0, 0, 0, 7] = v[B - 1, rows - 1, 0, 7] = 0
+        given.append(x.clone())
+        for b, r in ((0, 0), (B - 1, rows - 1)):
+            given[-1].view(B, rows, 3, D)[b, r, 0, 7] = float("inf")
+    # an infinity does not count for the scale, and under a scale of 0 it is coded as 0
+    for x, (_, scales) in zip(c.rows, c.want()[0]):
+        for b, r in ((0, 0), (B - 1, rows - 1)):
+            at = start + r
+            if scales[c.table[b, at // page], at % page // block, 0] > 0:
+                x.view(B, rows, 3, D)[b, r, 0, 7] = float("inf")
+    want, flags = c.want()
+    c.rows = given
+    assert c.run(plain=rows == 1) == flags | R.BAD_VALUE
+    c.same(want)

@@ -162,7 +162,7 @@ int split_ctas(int (&n)[2])
 // clusters of them only about 14 are placed at once).  Measured at the time, E4M3,
 // one KV head: one sequence of 1024 tokens 5.7 us with 8 x 8 warps, 6.7 us with 8 x
 // 4; 16 sequences of 512 tokens 6.0 us with 4 x 8 warps, 6.4 us with 8 x 4, 9.5 us
-// with 8 x 8 (now 4.9 and 5.1 us with the chosen ones).
+// with 8 x 8 (now 5.1 and 5.3 us with the chosen ones).
 void choose_cluster(int64_t segments, int64_t tiles, int& cluster, int& warps)
 {
     cluster = 8;
@@ -177,10 +177,11 @@ void choose_cluster(int64_t segments, int64_t tiles, int& cluster, int& warps)
 // sequences' tiles evenly, for about 5 us more.  So clusters whose warps have up to
 // six more tiles than the split ones (a quarter more when there are many) are
 // faster.  Only the longest length that may come is known here.  Measured with equal
-// lengths, split / cluster: 1 x 8192 tokens x 1 KV head 11.1 / 13.2 us, 16 x 8192
-// 22.4 / 26.9 us, x 4 KV heads 52 / 46 us, 64 x 8192 x 4 175 / 161 us; with lengths
-// of 0 to 8192: 8 x 4 20.7 / 22.6 us, 16 x 4 31.8 / 37.2 us, 64 x 4 91 / 128 us.  Of
-// those batches the rule splits 1 x 1, 16 x 1 and 64 x 4.
+// lengths, split / cluster: 1 x 8192 tokens x 1 KV head 10.2 / 14.4 us, 16 x 8192
+// 21.8 / 29.3 us, x 4 KV heads 51 / 46 us, 64 x 8192 x 4 171 / 160 us; with lengths
+// of 0 to 8192: 8 x 4 21.0 / 24.9 us, 16 x 4 32.0 / 39.2 us, 64 x 4 92 / 135 us.  Of
+// those batches the rule splits 1 x 1, 16 x 1 and 64 x 4: the slower way for 64 x 4 of
+// equal and for 8 x 4 and 16 x 4 of ragged lengths.
 bool split_pays(const ScaledDecodeArgs& a, int C)
 {
     const double tiles = (a.max_seq_len + kTile - 1.0) / kTile;
@@ -189,8 +190,8 @@ bool split_pays(const ScaledDecodeArgs& a, int C)
 }
 
 // Groups of split CTAs that the KV heads are dealt to: as many as divide them and
-// leave no more than one CTA in 24 without work (4 KV heads, 16 x 12K-16K tokens:
-// four groups 77.9 us, one 79.2 us).
+// leave no more than one CTA in 24 without work (4 KV heads, 16 x 12K-16K tokens, at
+// the time: four groups 77.9 us, one 79.2 us).
 int split_groups(int Hkv, int C)
 {
     for (int m = std::min(Hkv, C);; --m)

@@ -9,21 +9,23 @@
 // again when it grew.  A stored scale may be smaller than any made here, or for E4M3 no
 // power of two: units for which that arithmetic is not exact take a longer way.
 //
-// Bound: HBM, each source row read once and its codes written once (8190 rows x 4
-// heads x K and V: 6.4 us; it takes 15.4 us for E4M3 in blocks of 64, 18.3 us for
-// INT8, the first blocks' stored rows coded again).  What is left is latency:
-// finding the unit, its rows, the joint maximum and the stores follow one another
-// within a CTA, and about 16 warps per SM overlap.  A unit is one (block with new
-// rows, KV head, K or V); the block's first new row leads it.  Where a unit has one
-// new row (a decode step, blocks of one token) warps take units on their own
-// (append_rows_kernel: 16 rows 2.0 us, 2.8 us by CTAs; 8190 rows in blocks of one
-// token 18.4 us, 64 us by CTAs).  Else a CTA takes units of one leader, kWarpsPer
-// warps to a unit, enough that a warp's rows of the block stay in its registers
-// between the maximum and the codes (up to 64 rows a unit; longer blocks are read
-// twice, from L2 the second time), and looks through `chunk` consecutive rows for
-// leaders.  A loop over a leader's units, the next one's rows prefetched, was slower
-// (14 and 20 us at the time against 12 and 16: registers for two units, fewer CTAs);
-// so was reading rows twice to fit more CTAs (four rows held: 20 us).
+// Bound: HBM, each source row read once and its codes written once (6825 rows of 16
+// bits, what ragged cuts leave of 8190 on average, x 4 heads x K and V: 6.4 us; they
+// take 15.3 us for E4M3 in blocks of 64, 18.3 us for INT8, and 5.5 and 6.4 us more where
+// the scales of the sequences' first blocks grow and their stored rows are coded again).
+// What is left is latency: finding the unit, its rows, the joint maximum and the stores
+// follow one another within a CTA, and about 16 warps per SM overlap.  A unit is one
+// (block with new rows, KV head, K or V); the block's first new row leads it.  Where a
+// unit has one new row (a decode step, blocks of one token) warps take units on their
+// own (append_rows_kernel: 16 rows 2.1 us, 2.8 us by CTAs, and where scales grow 2.8 us
+// more for E4M3 and 7.3 us for INT8; 8190 rows in blocks of one token 19.7 us, 64 us by
+// CTAs).  Else a CTA takes units of one leader, kWarpsPer warps to a unit, enough that a
+// warp's rows of the block stay in its registers between the maximum and the codes (up
+// to 64 rows a unit; longer blocks are read twice, from L2 the second time), and looks
+// through `chunk` consecutive rows for leaders.  A loop over a leader's units, the next
+// one's rows prefetched, was slower (14 and 20 us at the time against 12 and 16:
+// registers for two units, fewer CTAs); so was reading rows twice to fit more CTAs (four
+// rows held: 20 us).
 #include <cfloat>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -697,14 +699,14 @@ template <class T, bool kInt8>
 cudaError_t append_typed(const AppendArgs& a, cudaStream_t s)
 {
     // One unit to a warp while they are few, then as many as fit its registers
-    // (8190 rows x 8 units, blocks of one token, E4M3: eight units 18.4 us, four
-    // 19.8, two 31 and one 43 us; 1024 rows: eight 4.6 us, one 3.9 us).
+    // (8190 rows x 8 units, blocks of one token, E4M3, at the time: eight units 18.4 us,
+    // four 19.8, two 31 and one 43 us; 1024 rows: eight 4.6 us, one 3.9 us).
     if (a.offs == nullptr || a.sc.block == 1)
         return (int64_t)a.T * 2 * a.Hkv <= kRowWarps ? append_rows<T, kInt8, 1>(a, s)
                                                      : append_rows<T, kInt8, 16 / sizeof(T)>(a, s);
     constexpr int kMost = kAppendWarps<T>;
-    // short blocks: fewer rows held, more CTAs (8190 rows, E4M3, blocks of four 14.5
-    // us, 22 us with sixteen held; of eight 13.9 and 16.7 us)
+    // short blocks: fewer rows held, more CTAs (8190 rows, E4M3, blocks of four 14.8
+    // us, 22 us with sixteen held; of eight 14.0 and 16.7 us)
     if (a.sc.block <= 4)
         return append_run<T, kInt8, 1, 4>(a, s);
     if (a.sc.block <= 8)

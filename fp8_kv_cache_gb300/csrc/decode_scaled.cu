@@ -14,8 +14,8 @@
 //    time.  A CTA that has all tiles of a segment writes its rows; the others leave
 //    partial results (n, d, O) in slots that the merge kernel, a programmatic
 //    dependent of the split kernel, joins in a fixed order.
-// 16 sequences of 12K to 16K tokens, 4 KV heads: E4M3 77.9 us, INT8 79.3 us (0.90
-// of the measured copy bandwidth); 8 of 1024 tokens 6.6 us, one of 64 3.6 us.
+// 16 sequences of 12K to 16K tokens, 4 KV heads: E4M3 78.0 us (0.90 of the measured
+// copy bandwidth), INT8 81.6 us; 8 of 1024 tokens 6.9 us, one of 64 3.6 us.
 #include <algorithm>
 #include <atomic>
 

@@ -284,7 +284,7 @@ cudaError_t logits_typed(LogitsArgs a, cudaStream_t s)
     // Each row is cut into equal shares of columns, a CTA each, as many as fill the
     // SMs once, or w times in turn where shares would pass `most` (16 x 248,320,
     // 4096 tokens of history: 304 CTAs of 13,088 columns 9.8 us, 496 of 8192, which
-    // is 1.6 waves, 11.4 us; 400 rows of 248,320 144 us and 173 us).
+    // is 1.6 waves, 11.4 us; 400 rows of 248,320 140 us and 173 us).
     auto share = [&](int64_t slots, int64_t most) {
         const int64_t w = ((a.V + most - 1) / most * a.B + slots - 1) / slots, k = slots * w / a.B;
         return (int)std::max<int64_t>(((a.V + k - 1) / k + 31) / 32 * 32, 2048);
@@ -292,7 +292,7 @@ cudaError_t logits_typed(LogitsArgs a, cudaStream_t s)
     a.cols = share(2 * kSms, kLogitCols / 2);
     // Every CTA reads its row's whole history: where that is half as long as the
     // share or more, one CTA of 1024 threads per SM in place of two of 512 (32,768
-    // tokens 15.5 us and 18.2 us), unless they would have too few columns and a
+    // tokens 14.8 us and 18.2 us), unless they would have too few columns and a
     // history that half the threads load at once (one row, 4096 tokens: 3.8 and 3.3).
     const int64_t history = a.r.history != nullptr ? a.r.max_history : 0;
     const int wide = share(kSms, kLogitCols);

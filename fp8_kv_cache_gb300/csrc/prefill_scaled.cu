@@ -3,13 +3,13 @@
 // The operation of the per-tensor prefill (each row attends to its selected
 // four-token blocks and its causal tail), with the scores and weights of
 // scaled_core.cuh.  Bound: the tiles' instructions, fed by a gather of every
-// row's own blocks out of L2 at 11.5 TB/s.
+// row's own blocks out of L2 at 10.4 TB/s.
 // One CTA per (query row, KV head), or a cluster of up to 8 when there are few rows;
 // it resolves a chunk of block entries into a shared-memory table (first token,
 // page), so that the ring fills need no dependent global load, and its warps take
-// 16-token tiles in turn.  4096 rows of 512 blocks 378 us (E4M3), 456 us (INT8).  One
-// row of 512 blocks 7.3 us (39 us by one CTA, with the tiles of the time), 64 rows
-// 14.4 us (40 us), 128 rows 22 us (40 us).
+// 16-token tiles in turn.  4096 rows of 512 blocks 419 us (E4M3), 497 us (INT8).  One
+// row of 512 blocks 7.8 us (39 us by one CTA, with the tiles of the time), 64 rows
+// 15.1 us (40 us), 128 rows 24 us (40 us).
 #include <atomic>
 
 #include "scaled_core.cuh"

@@ -14,8 +14,8 @@
 // binary16, so a weight is fed as the sum of two such numbers, its rounding and the
 // rounding of what that leaves: 22 bits, below the float32 errors of the scores.
 // (One number, 11 bits, moved outputs by as much as their own rounding to binary16
-// does: 64 tokens, errors of 2.5e-4 instead of 2.1e-4; prefill took 378 us for the
-// 414 below, decode 6.6 for 6.9.)  They are fed as 2^kShift p_t: binary16's steps
+// does: 64 tokens, errors of 2.5e-4 instead of 2.1e-4; prefill took 378 us for
+// 414, decode 6.6 for 6.9.)  They are fed as 2^kShift p_t: binary16's steps
 // end at 2^-24, which then stands for 2^-(24 + kShift).  The denominator is summed
 // from the float32 weights.  Scales below 2^-80 count as 2^-80 in log2 vs: their
 // values are zeros in binary16 either way, and the denominator stays finite.
@@ -28,7 +28,7 @@
 // their rows.
 //
 // Bound where the codes come from L2 (prefill): instructions.  4096 rows x 2050
-// E4M3 tokens x 6 heads take 414 us.  At one binary16 number a weight they took 378
+// E4M3 tokens x 6 heads take 419 us.  At one binary16 number a weight they took 378
 // us; 408 us with 64-bit row offsets and four chains of score sums; 531 us also with
 // fills of half tiles, a joint maximum over the lanes for every tile (now only when
 // one passes the reference by 2^kSlack) and V's bytes paired by permutes; 80 us more

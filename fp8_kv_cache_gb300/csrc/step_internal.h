@@ -78,12 +78,13 @@ struct CacheArgs {
     const float *ks, *vs;
 };
 
-// The block-scaled decode's split kernel.  Five warps a CTA, two CTAs per SM, take
-// 77.9 us for 16 x 12K-16K tokens of 4 KV heads (E4M3; INT8 79.3), 133.5 us for 64 x
-// 4K-8K and 20.1 us for seven ragged INT8 sequences; six warps 79.8 (80.4), 135.8 and
-// 19.9 us, four 77.2 (81.4), 141.7 and 26.7 us; four warps and three CTAs 103 us, ten
-// and one 81 us.  Virtual tiles charged for a piece's start when the line of tiles is
-// cut: 12 took 0.8 % longer, 20 the same.  At least eight tiles a CTA.
+// The block-scaled decode's split kernel: five warps a CTA, two CTAs per SM.  With weights
+// of 11 bits these took 77.9 us for 16 x 12K-16K tokens of 4 KV heads (E4M3; INT8 79.3),
+// 133.5 us for 64 x 4K-8K and 20.1 us for seven ragged INT8 sequences (78.0, 81.6 and 20.5
+// us now); six warps 79.8 (80.4), 135.8 and 19.9 us, four 77.2 (81.4), 141.7 and 26.7 us;
+// four warps and three CTAs 103 us, ten and one 81 us.  Virtual tiles charged for a
+// piece's start when the line of tiles is cut: 12 took 0.8 % longer, 20 the same.  At
+// least eight tiles a CTA.
 constexpr int kSplitWarps = 5;
 constexpr int kSplitPieceTiles = 16;
 constexpr int kSplitMinTiles = 8;
